@@ -7,25 +7,29 @@
 // column that trails the running maximum:
 //   P_c = 2^{y_c - r},  O = sum_c P_c x_c[0:512],  l = sum_c P_c / g_c,
 //   out = O / l,  lse = ln 2 (r + log2 l).
-// r is set to the exact maximum less 5, and again when a score passes it by 8.75 (P <= 2^8.75
-// < 448, the largest e4m3 value): on a segment's first tile and seldom after (of scores with
-// a deviation of 2.5 in base 2, about one tile in a hundred, of the first twenty one in ten or
-// twelve; less 7, one in ten throughout), so that most
-// tiles need no column maximum, no second barrier and no rescale of O.
+// r is set to the exact maximum less 7, and again when a score passes it by 12 (P <= 2^12): on a
+// segment's first tile and seldom after, so that most tiles need no column maximum, no second
+// barrier and no rescale of O.  (Less 8: bs 8, 1k-4k 78.5 us against 76.0, bs 1, 185k 380 against
+// 374; less 6: 73.6 and 371, with the weights' full precision a binary order less deep.)
 // No value is dequantised: the codes go from HBM into the matrix instructions as they are.
-// q and P have to be e4m3 operands too and are each the sum of two:
+// q and P have to be 8-bit operands too and are each the sum of two:
 // - q (split_q_row, in the planner's launch): a row is scaled by a power of two to a largest
 //   value in [128, 256) and taken as hi = e4m3(q), lo = e4m3(q - hi).  A bf16 value has 8
-//   significant bits and e4m3 4, so hi + lo is q exactly down to 2^-10 of the row's largest
-//   value, and within 2^-18 of that value below; products and sums are fp32.  hi and lo are
+//   significant bits and e4m3 4, so hi + lo is q exactly down to 2^-9 of the row's largest
+//   value, and within 2^-17 of that value below (half of e4m3's smallest step, 2^-9, to at
+//   least 128); products and sums are fp32.  hi and lo are
 //   stacked as 128 columns of one instruction, the width that the tensor cores need for their
 //   full rate (64.7 clocks an instruction, as for 64 columns), so the exact scores cost no
 //   more than rounded ones would.
-// - P in [0, 431] likewise, off by at most 2^-8 of its value (a bf16's half step).  Below 2^-6
-//   both parts have e4m3's smallest step, 2^-9; to keep the rounding of many small equal
-//   weights from adding up, lo is rounded after adding an offset spread evenly over one step
-//   across the tile's rows (the bit-reversed row number), so that a tile's mean is right to
-//   a 128th of a step, 2^-21 of the largest weight.
+// - P in [0, 2^12] as an e4m3 and an e5m2 value (split_weights).  Either may be the coarse part.
+//   From 2^-6 up, 13 binary orders below a fresh reference's maximum and more below a later
+//   one, the sum is off by at most 2^-8 of P (half a step of its finer part) and 2^-11 of the
+//   f16 it starts from: what bf16 weights are off by.  Below, e4m3 nears its smallest step,
+//   2^-9, and e5m2 keeps 3 bits down to 2^-14: rounded to nearest P would be off by up to an
+//   eighth, alike for alike weights.  There lo is rounded up or down at random (a hash of the
+//   key column; off by up to a quarter of P, to the right mean), so that the errors of many small
+//   weights average out whatever they multiply.  (An offset that went by the row of the tile
+//   kept the sum of the weights and lost values that repeat with position.)
 //
 // Layout on the SM.  One CTA per SM walks its share of (column group, key tile) units, as the
 // 16-bit kernel does (plan, partial slots and merges are shared).  A key tile is 128 rows of
@@ -35,17 +39,17 @@
 // The 16-bit kernel has room for one tile and runs gather, scores, softmax and values in
 // sequence.  Transposed products, key rows and value dims on the TMEM lanes:
 //   S^T[128 keys][64 hi | 64 lo] = X . Q^T      (18 MMAs 128x128x32; two buffers)
-//   O^T[512 dims][64 columns]   += X^T . P^T    (4 blocks x (hi, lo) x 4 MMAs 128x64x32)
-// P^T hi goes over the tile's rope chunk, which the scores no longer need, lo into its own
+//   O^T[512 dims][64 columns]   += X^T . P^T    (4 blocks x (e4m3, e5m2) x 4 MMAs 128x64x32)
+// P^T hi (e4m3) goes over the tile's rope chunk, which the scores no longer need, lo into its own
 // 8 KB.
 //
 // Warp roles: warps 0-3 gather rows (cp.async) and scales, warp 0 also loads q (TMA); one thread
 // of warp 12 issues the scores and one of warp 13 the values, so that neither waits for the
 // other's turn; warps 4-11 run the softmax, the rescale and the epilogue.
 //
-// Measured.  64 requests of 8k-64k keys, trees of 1 to 16 drafts: 2.50 ms, 1.01 PFLOP/s of
+// Measured.  64 requests of 8k-64k keys, trees of 1 to 16 drafts: 2.53 ms, 1.00 PFLOP/s of
 // attention arithmetic, 53% of the measured bf16 matrix peak; one request of 185k keys with 16
-// drafts: 366 us, 59%.  A tile takes about 2.2 us (4300 clocks at 64 heads): its 50 MMAs 2750
+// drafts: 374 us, 58%.  A tile takes about 2.2 us (4300 clocks at 64 heads): its 50 MMAs 2750
 // clocks when nothing is waited for, the softmax 1700.  What bounds it is the cycle of one tile
 // buffer, two tiles long: values 3000 clocks (the scores of the next tile share the tensor
 // cores), the refill of the chunks released last 1800, their scores 600, the softmax, and about
@@ -94,18 +98,19 @@ static_assert(sizeof(SegInfo) <= 48, "segment info block");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;             // S^T of tile buffer b at 256 + 128 b; O^T at 0..255
 constexpr uint32_t kErrBadScale = 16u;
-constexpr float kPBits = 5.f;               // P = 2^5 at a fresh reference's maximum
-constexpr float kLag = 3.75f;               // how far (base 2) scores may rise above it
+constexpr float kPBits = 7.f;               // P = 2^7 at a fresh reference's maximum
+constexpr float kLag = 5.f;                 // how far (base 2) scores may rise above it
 constexpr float kNoKey = -3e38f;            // reference of a column that has seen no key
 constexpr uint32_t kHalfBar = 2;            // named barriers 2, 3: the four warps of a half
 
-// Instruction descriptor of kind::f8f6f4 with e4m3 A and B and fp32 D.
+// Instruction descriptors of kind::f8f6f4 with e4m3 A and B, or for kIdescPV5 e5m2 B, and fp32 D.
 constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
 constexpr uint32_t kIdescQK = idesc_e4m3(128, 128, 0, 0);
-constexpr uint32_t kIdescPV = idesc_e4m3(128, 64, 1, 1);
+constexpr uint32_t kIdescPV4 = idesc_e4m3(128, 64, 1, 1);
+constexpr uint32_t kIdescPV5 = kIdescPV4 | (1u << 10);   // B is e5m2
 
 // Shared-memory matrix descriptors (address and leading stride in the low word, 8-row stride,
 // version and swizzle in the high word).  An MMA takes low words as a base and a constant
@@ -362,8 +367,8 @@ __device__ void value_issuer(const Problem& p, unsigned char* sm, Bars* bars, vo
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           const uint32_t voff = (ks * 4096) >> 4, poff = (ks * 2048) >> 4;
-          mma_e4m3(tmem + 64 * m, vm, voff, kDescSw128, hi_lo, poff, kDescSw64, kIdescPV, ks > 0 || !first);
-          mma_e4m3(tmem + 64 * m, vm, voff, kDescSw128, lo_lo, poff, kDescSw64, kIdescPV, 1);
+          mma_e4m3(tmem + 64 * m, vm, voff, kDescSw128, hi_lo, poff, kDescSw64, kIdescPV4, ks > 0 || !first);
+          mma_e4m3(tmem + 64 * m, vm, voff, kDescSw128, lo_lo, poff, kDescSw64, kIdescPV5, 1);
         }
         ptx::mma_commit(&bars->kv_empty[buf][m]);
       }
@@ -385,6 +390,21 @@ failed:
 __device__ __forceinline__ uint32_t scrub4(uint32_t w) {
   const uint32_t nan = __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
   return w & ~nan;
+}
+
+// Two weights (P, at most 2^12) as the sums of an e4m3 value (codes in the low 16 bits of hi) and
+// an e5m2 value (codes in bytes 1 and 3 of lo: e5m2 is the upper byte of f16).  From 1 up e5m2
+// takes the coarse part and e4m3, whose range ends at 448, what is left of it (at most 2^8);
+// below, e4m3 takes the coarse part.  What e4m3 leaves is rounded to e5m2 to nearest by adding
+// half of its last step, or where P is below 2^-6 by adding the random offset of `dither`.
+__device__ __forceinline__ void split_weights(__half2 y, uint32_t dither, uint32_t& hi, uint32_t& lo) {
+  const uint32_t coarse = (*(const uint32_t*)&y + 0x00800080u) & 0xff00ff00u & __hge2_mask(y, __float2half2_rn(1.f));
+  const __half2 rest = __hsub2(y, *(const __half2*)&coarse);
+  hi = q8::pack2(*(const uint32_t*)&rest);
+  const uint32_t back = q8::unpack2(hi);
+  const __half2 left = __hsub2(y, *(const __half2*)&back);
+  const uint32_t small = __hlt2_mask(y, __float2half2_rn(0x1p-6f));
+  lo = *(const uint32_t*)&left + ((dither & small) | (0x00800080u & ~small));
 }
 
 // ---- merging a column group's partials ----
@@ -562,9 +582,6 @@ __device__ void softmax_role(const Problem& p, unsigned char* sm, Bars* bars, vo
   int32_t* slots_s = (int32_t*)(sm + kSlotOff);
   SegInfo* si = (SegInfo*)(sm + kSegOff);
   const int64_t q_first = p.qo_indptr[0];
-  // (2k + 1 - 128) / 128 half steps of 2^-9, k the bit-reversed row: inside half a step, so
-  // that a weight of 0 stays 0
-  const __half2 spread = __float2half2_rn((float)(int)(2 * (__brev(row) >> 25) + 1 - 128) * 0x1p-17f);
   uint32_t tl = 0, sc = 0;
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -626,6 +643,10 @@ __device__ void softmax_role(const Problem& p, unsigned char* sm, Bars* bars, vo
           v2[2 * i + 1] = ptx::add_f32x2(n.y, lg2);
         }
       }
+      // random bits of the key column, for the rounding of small weights (split_weights)
+      uint32_t dither = (uint32_t)c * 0x9e3779b1u;
+      dither = (dither ^ (dither >> 16)) * 0x9e3779b1u;
+      dither = (dither >> 24) | (dither & 0x00ff0000u);
       wait(&bars->s_full[buf], par);
       __syncwarp();
       ptx::tc_fence_after();
@@ -771,16 +792,9 @@ __device__ void softmax_role(const Problem& p, unsigned char* sm, Bars* bars, vo
         lp[4 * i4 + 3] = fmaf(e3, inv_g, lp[4 * i4 + 3]);
         uint32_t w[2], v[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const __half2 y = __floats2half2_rn(k ? e2 : e0, k ? e3 : e1);
-          const uint32_t hc = q8::pack2(*(const uint32_t*)&y);
-          const uint32_t back = q8::unpack2(hc);
-          const __half2 rest = __hadd2(__hsub2(y, *(const __half2*)&back), spread);
-          w[k] = hc;
-          v[k] = q8::pack2(*(const uint32_t*)&rest);
-        }
+        for (int k = 0; k < 2; ++k) split_weights(__floats2half2_rn(k ? e2 : e0, k ? e3 : e1), dither, w[k], v[k]);
         phi[i4] = w[0] | (w[1] << 16);
-        plo[i4] = v[0] | (v[1] << 16);
+        plo[i4] = __byte_perm(v[0], v[1], 0x7531);
       }
       unsigned char* hi_dst = tile + 4 * kChunk;
       unsigned char* lo_dst = sm + kPLoOff;
