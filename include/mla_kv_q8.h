@@ -102,7 +102,14 @@ size_t mla_tree_verify_q8_workspace_bytes(int32_t bs, int32_t max_q_per_req, int
  *   s_c = sm_scale * g(c) * <q[r,h,0:576], code(c)[0:576]>
  *   out[r,h,0:512] = softmax over visible c of s_c, applied to g(c) * code(c)[0:512]
  * A NaN code in a row that a query token does not see does not reach that token's output;
- * one in a row that it sees makes its output and lse NaN.  Reads the device error bits with
+ * one in a row that it sees makes its output and lse NaN.
+ * Precision, beside fp32 sums and out's bf16: a query row's values are exact down to 2^-9 of its
+ * largest and within 2^-17 of that below; a key's weight w_c is off by at most 2^-8 + 2^-11 of
+ * itself, as in bf16, while w_c g(c) is at least 2^-13 of the largest w g of the column's keys
+ * that hold any latent value, and smaller ones are rounded at random to the right mean (off by at
+ * most a quarter, and from 2^-21 on down by a step of 2^-23 of that largest).  lse does not depend
+ * on those roundings.  The same call gives the same bits.
+ * Reads the device error bits with
  * mla_tree_verify_read_device_status(); MLA_TV_DEV_BAD_SCALE may be among them.
  */
 int mla_tree_verify_q8(const void* q, const void* kv_cache, const float* scales,

@@ -11,6 +11,9 @@
 // segment's first tile and seldom after, so that most tiles need no column maximum, no second
 // barrier and no rescale of O.  (Less 8: bs 8, 1k-4k 78.5 us against 76.0, bs 1, 185k 380 against
 // 374; less 6: 73.6 and 371, with the weights' full precision a binary order less deep.)
+// A key whose latent codes are all zero (a row of zeros has scale 1, whatever the others') counts in l
+// and adds nothing to O: any g_c would do for it, and where references are set it is taken as
+// 2^-60, so that its own does not push the other keys' weights out of P's range.
 // No value is dequantised: the codes go from HBM into the matrix instructions as they are.
 // q and P have to be 8-bit operands too and are each the sum of two:
 // - q (split_q_row, in the planner's launch): a row is scaled by a power of two to a largest
@@ -100,6 +103,7 @@ constexpr uint32_t kSCol = 256;             // S^T of tile buffer b at 256 + 128
 constexpr uint32_t kErrBadScale = 16u;
 constexpr float kPBits = 7.f;               // P = 2^7 at a fresh reference's maximum
 constexpr float kLag = 5.f;                 // how far (base 2) scores may rise above it
+constexpr float kEmptyBits = 60.f, kEmptyInv = 0x1p60f;   // scale 2^-60 of a key without values
 constexpr float kNoKey = -3e38f;            // reference of a column that has seen no key
 constexpr uint32_t kHalfBar = 2;            // named barriers 2, 3: the four warps of a half
 
@@ -628,7 +632,7 @@ __device__ void softmax_role(const Problem& p, unsigned char* sm, Bars* bars, vo
       wait(&bars->sc_full[buf], par);
       const float g = ((const float*)(sm + kScaleOff))[buf * 128 + row];   // 0: no valid key
       if (!(g > 0.f)) vq = 0u;
-      const float lg = g > 0.f ? __log2f(g) : 0.f, inv_g = g > 0.f ? __frcp_rn(g) : 0.f;
+      float lg = g > 0.f ? __log2f(g) : 0.f, inv_g = g > 0.f ? __frcp_rn(g) : 0.f;
       // y less the reference is (hi + lo) u + v; u and v while the scores are not there yet
       uint64_t u2[16], v2[16];
       {
@@ -693,6 +697,17 @@ __device__ void softmax_role(const Problem& p, unsigned char* sm, Bars* bars, vo
       // The four warps that share these 32 columns agree on whether a score rose too far
       // above its column's reference (a segment's first keys always do).
       if (__builtin_expect(ptx::bar_any(kHalfBar + half, 128, top > kPBits + kLag), 0)) {
+        // A row without values gets the scale 2^-60 in place of its own.
+        uint32_t any = vq == 0u;
+#pragma unroll 1
+        for (int gq = 0; gq < 32 && any == 0u; ++gq) {
+          const uint4 w = *(const uint4*)(tile + (gq >> 3) * kChunk + swz(row, gq & 7));
+          any = (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
+        }
+        if (any == 0u) {
+          lg = -kEmptyBits;
+          inv_g = kEmptyInv;
+        }
         // New references: each column's exact maximum so far.  Each warp reduces its 32 rows;
         // lane i of the half's quarter-0 warp folds the quarters into column hb + i.
         // y itself: nothing of it is left beside the reference of a column without keys

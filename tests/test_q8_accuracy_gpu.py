@@ -92,3 +92,45 @@ def test_scores_that_rise_under_the_reference():
         b.kv[at[k]] = codes(rows[i])
     out, lse = b.run(sm_scale=scale)
     q8_tight.check(b, out, lse, sm_scale=scale, alike=True)
+
+
+@pytest.mark.parametrize("heads", [64, 8])
+@pytest.mark.parametrize("amplitude", [1.0, 1e-2, 1e-4, 1e-6])
+@pytest.mark.parametrize("kind", ["zeros", "half", "rope"])
+def test_rows_without_values_among_small_ones(kind, amplitude, heads):
+    """A visible row whose latent codes are all zero and whose scale is 1 (what kv_append stores for
+    a row of zeros; with rope values too) adds nothing to the output, and takes no precision
+    from keys whose scales are far smaller."""
+    b = Batch([301, 40], [3, 1], heads, seed=34)
+    b.scales *= amplitude
+    at = b.kv_indices.long()
+    at = at[::2] if kind == "half" else at[[7, 150, 310]]
+    b.kv[at] = 0
+    b.scales[at] = 1.0
+    b.kv[at[::2], :LATENT] = 0x80            # minus zero
+    if kind == "rope":
+        b.kv[at, LATENT:] = codes(4 * torch.randn((at.numel(), ROW - LATENT), device="cuda"))
+    out, lse = b.run()
+    q8_tight.check(b, out, lse)
+    assert b.flags() == 0
+
+
+@pytest.mark.parametrize("first", [True, False])
+def test_a_row_without_values_that_outweighs_the_others(first):
+    """Scores of -30 for the keys with values, 0 for the one without: outputs of about e^-30, and
+    in the other order of tiles."""
+    b = Batch([600], [2], 64, seed=35)
+    at = torch.cat([b.kv_indices.long(), b.out_cache_loc])
+    b.kv[at, 0] = 0x77                        # 240
+    b.q[..., 0] = -1
+    b.scales[:] = 1 / 240
+    empty = at[3 if first else 500]
+    b.kv[empty] = 0
+    b.scales[empty] = 2.0 ** 20
+    out, lse = b.run(sm_scale=30.0)
+    q8_tight.check(b, out, lse, sm_scale=30.0)
+    only = Batch([200], [1], 64, seed=36)     # nothing but rows without values
+    at = torch.cat([only.kv_indices.long(), only.out_cache_loc])
+    only.kv[at] = 0
+    out, lse = only.run()
+    assert not out.any() and float((lse - math.log(201)).abs().max()) < 1e-5
