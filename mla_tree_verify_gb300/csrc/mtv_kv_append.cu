@@ -96,6 +96,11 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const RowIn& in,
     *(uint4*)(dst + 8 * lane) = w0;
     *(uint4*)(dst + 256 + 8 * lane) = w1;
     const uint32_t y = bf16x2(ya, yb);
+    // an exponent of ones (NaN, infinity) carries into the sign's place
+    auto ones = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+    const uint32_t bad = ones(w0.x) | ones(w0.y) | ones(w0.z) | ones(w0.w) | ones(w1.x) | ones(w1.y) |
+                         ones(w1.z) | ones(w1.w) | ones(y);
+    if (bad & 0x80008000u) atomicOr(a.status, kBadValue);
     if constexpr (kInter) {
       *(uint32_t*)(dst + kDv + 2 * lane) = y;
     } else {

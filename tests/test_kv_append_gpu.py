@@ -194,6 +194,36 @@ def test_nonfinite_rows(value, dim):
     assert bool(((values(c.kv[c.slots])[:, :LATENT] - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -10).all())
 
 
+@pytest.mark.parametrize("heads", [0, 8, 64])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dim", [0, 1, 255, 256, 511, 512, 520, 575])
+def test_nonfinite_rows_of_a_bf16_cache(value, dim, heads):
+    """Flagged, and written as they are; the other rows and the queries as ever."""
+    c = Case(10, heads, e4m3=False, seed=9)
+    (c.latent if dim < LATENT else c.k_pe)[4, dim if dim < LATENT else dim - LATENT] = value
+    c.run()
+    assert int(c.status) == mtv.APPEND_BAD_VALUE
+    row = c.kv[c.slots[4]]
+    assert torch.equal(row[:LATENT].view(torch.int16), c.latent[4].view(torch.int16))
+    assert bool(row[LATENT:].isfinite().all()) == (dim < LATENT)
+    c.kv[c.slots[4]] = c.latent[4] = c.k_pe[4] = 0
+    c.check(False)
+
+
+def test_largest_values_of_a_bf16_cache_are_not_flagged():
+    c = Case(5, 0, e4m3=False, seed=12)
+    big = torch.finfo(torch.bfloat16).max
+    c.latent[0], c.latent[1, ::2], c.k_pe[:] = big, -big, 0
+    c.run()
+    c.check(False)
+    assert int(c.status) == 0
+    c.k_pe[3] = big                # rotated by an angle whose cosine and sine add up to more than 1
+    c.cs[c.pos[3]] = 0.75
+    c.status.zero_()
+    c.run()
+    assert int(c.status) == mtv.APPEND_BAD_VALUE and bool(c.kv[c.slots[3], LATENT:].isinf().any())
+
+
 def test_rotation_in_place_and_on_another_stream():
     c = Case(60, 16, seed=10)
     c.q[..., LATENT:].copy_(c.q_pe)
