@@ -66,7 +66,8 @@ extern "C" {
  *                position outside [0, max_pos)): such a token is skipped like padding;
  *                _BAD_VALUE: a row holds a NaN or an infinity, or computed scales would pass
  *                2^40 (with computed scales the row is written as NaN codes with scale 1, so
- *                that attention that sees it gives NaN; a bf16 row is written as it is);
+ *                that attention that sees it gives NaN; with given scales the values that are
+ *                NaN or infinite become NaN codes; a bf16 row is written as it is);
  *                _BAD_SCALE: a given scale is NaN or
  *                outside [2^-40, 2^40] (the token is skipped)
  *

@@ -90,7 +90,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const RowIn& in,
   float x[16];
   widen8(w0, *(float(*)[8])x);
   widen8(w1, *(float(*)[8])(x + 8));
-  const float ya = ra * c - rb * s, yb = rb * c + ra * s;
+  float ya = ra * c - rb * s, yb = rb * c + ra * s;
   if constexpr (kType == 0) {
     uint16_t* dst = (uint16_t*)a.kv + slot * kDqk;
     *(uint4*)(dst + 8 * lane) = w0;
@@ -122,7 +122,14 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const RowIn& in,
         if (lane == 0) atomicOr(a.status, kBadScale);
         return;
       }
-      if (top >= 0x7f800000u && lane == 0) atomicOr(a.status, kBadValue);
+      if (top >= 0x7f800000u) {   // infinities become NaN: saturated, they would look like values
+        if (lane == 0) atomicOr(a.status, kBadValue);
+        auto drop = [](float v) { return v - v == 0.f ? v : __uint_as_float(0x7fffffffu); };
+        ya = drop(ya);
+        yb = drop(yb);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = drop(x[k]);
+      }
     } else {
       scale = amax > 0.f ? fmaxf(amax * (1.f / q8::kMax), q8::kScaleMin) : 1.f;
       poison = !(amax <= q8::kMax * q8::kScaleMax);

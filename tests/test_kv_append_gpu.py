@@ -224,6 +224,46 @@ def test_largest_values_of_a_bf16_cache_are_not_flagged():
     assert int(c.status) == mtv.APPEND_BAD_VALUE and bool(c.kv[c.slots[3], LATENT:].isinf().any())
 
 
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("heads", [0, 64])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dim", [0, 300, 511, 512, 520, 575])
+def test_nonfinite_rows_with_given_scales(value, dim, heads, block):
+    """Flagged; what is not finite becomes a NaN code, so that attention that sees the row gives NaN,
+    and the row's other values are stored as ever."""
+    c = Case(10, heads, block=block, seed=13)
+    (c.latent if dim < LATENT else c.k_pe)[4, dim if dim < LATENT else dim - LATENT] = value
+    c.run(given=True)
+    assert int(c.status) == mtv.APPEND_BAD_VALUE
+    s = c.slots[4]
+    nan = values(c.kv[s]).isnan()
+    if dim < LATENT:
+        want = torch.zeros(ROW, dtype=torch.bool, device="cuda")
+        want[dim] = True
+    else:       # the pair that holds it, both of whose values are sums with it
+        want = torch.zeros(ROW, dtype=torch.bool, device="cuda")
+        k = (dim - LATENT) // 2 * 2 + LATENT
+        want[k:k + 2] = True
+    assert torch.equal(nan, want)
+    c.kv[s] = torch.where(nan, 0, c.kv[s])
+    row = values(c.kv[s])
+    x = torch.cat([c.latent[4].double(), rot(c.k_pe[4].double(), c.cs[c.pos[4]].double(), True)])
+    x = (x / c.scales.double()[s // block]).clamp(-448, 448)
+    near = (row - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -10 + 2.0 ** -20 / float(c.scales[s // block])
+    assert bool(near[~want].all())
+    c.kv[s] = c.latent[4] = c.k_pe[4] = 0
+    c.check(True)
+
+
+def test_large_values_with_given_scales_are_saturated_and_not_flagged():
+    c = Case(6, 0, block=16, seed=14)
+    c.latent[2] = torch.finfo(torch.bfloat16).max
+    c.scales[:] = 2.0 ** -40
+    c.run()
+    c.check(True)
+    assert int(c.status) == 0
+
+
 def test_rotation_in_place_and_on_another_stream():
     c = Case(60, 16, seed=10)
     c.q[..., LATENT:].copy_(c.q_pe)
