@@ -3,6 +3,7 @@
 // stream.  No allocation, no synchronisation, no device reads on this path ("The
 // Architecture of Capture Safety", section "The Design Emerges": fixed grid,
 // preallocated workspace, raw pointers plus scalars).
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -177,7 +178,8 @@ int run(const void* q, const void* kv_cache, const int32_t* kv_indices, const in
   p.lanes = lanes;
   p.seg_cost = opt.q8 ? mtv::kSegCostQ8 : mtv::kSegCost;
   p.merge_mode = opt.merge_mode;
-  p.wait_ns = opt.wait_ns ? opt.wait_ns : kDefaultWaitNs;
+  // (the 8-bit kernel counts two clocks a nanosecond, in 64 bits)
+  p.wait_ns = opt.wait_ns ? std::min<uint64_t>(opt.wait_ns, UINT64_MAX / 4) : kDefaultWaitNs;
   p.num_slots = num_slots;
   p.total_q = total_q;
   p.num_kv_indices = num_kv_indices;
