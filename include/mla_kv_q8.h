@@ -90,8 +90,8 @@ int mla_kv_append(const void* latent, int64_t latent_stride, const void* k_pe, i
                   int64_t n, int32_t interleaved, uint32_t* status, cudaStream_t stream);
 
 /* Bytes of workspace of mla_tree_verify_q8(): that of mla_tree_verify() and room for the
- * split queries (bs * max_q_per_req * num_heads rows of 1156 bytes).  0 for invalid
- * arguments. */
+ * split queries (bs * max_q_per_req * num_heads rows of 1156 bytes, fewer than 2^30).  0 for
+ * arguments that the call refuses. */
 size_t mla_tree_verify_q8_workspace_bytes(int32_t bs, int32_t max_q_per_req, int32_t num_heads);
 
 /*

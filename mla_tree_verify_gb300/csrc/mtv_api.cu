@@ -110,6 +110,7 @@ struct WsQ8 {
   mtv::WsLayout base;
   size_t split_off, factor_off, total;
   int64_t rows;
+  bool fits() const { return rows <= INT32_MAX / 2; }   // 2 rows: tensor-map coordinates
 };
 
 WsQ8 ws_q8(int64_t bs, int64_t max_q, int64_t grid, int64_t heads) {
@@ -156,7 +157,7 @@ int run(const void* q, const void* kv_cache, const int32_t* kv_indices, const in
     return MLA_TV_ERR_SHAPE;
   const WsQ8 w8 = ws_q8(bs, max_q_per_req, grid, num_heads);
   const mtv::WsLayout& w = w8.base;
-  if (opt.q8 && w8.rows > INT32_MAX / 2) return MLA_TV_ERR_SHAPE;   // tensor-map coordinates
+  if (opt.q8 && !w8.fits()) return MLA_TV_ERR_SHAPE;
   if (workspace_bytes < (opt.q8 ? w8.total : w.total)) return MLA_TV_ERR_WORKSPACE;
 
   mtv::Problem p;
@@ -352,7 +353,8 @@ size_t mla_tree_verify_q8_workspace_bytes(int32_t bs, int32_t max_q_per_req, int
   if (mla_tree_verify_workspace_bytes(bs, max_q_per_req, num_heads) == 0) return 0;
   int dev;
   if (current_device(&dev) != MLA_TV_OK) return 0;
-  return ws_q8(bs, max_q_per_req, g_sm_count[dev], num_heads).total;
+  const WsQ8 w = ws_q8(bs, max_q_per_req, g_sm_count[dev], num_heads);
+  return w.fits() ? w.total : 0;
 }
 
 int mla_tree_verify_q8(const void* q, const void* kv_cache, const float* scales,
