@@ -139,6 +139,30 @@ int mla_tree_verify_q8_debug_ex(const void* q, const void* kv_cache, const float
                                 const mla_tree_verify_debug_opts* opts, cudaStream_t stream);
 
 /*
+ * mla_tree_verify_q8() with settings for the merge of the pieces that a query token's keys are
+ * cut into (test hooks; the output bits are the same with all of them):
+ *   merge_mode     MLA_TV_Q8_MERGE_AUTO: as timing allows (the normal call: the CTA of the last
+ *                  piece merges from TMEM if the others are done before it, else CTAs without
+ *                  work left share the merge).  _NO_TMEM: never from TMEM.  _ALONE: the CTA that
+ *                  finishes last merges, from the workspace and alone.
+ *   help_limit_ns  how long a CTA without work left waits for the other pieces before it leaves
+ *                  the merge to others: 0 the library's choice (40 us), at most 10^9
+ * Others give MLA_TV_ERR_SHAPE.
+ */
+#define MLA_TV_Q8_MERGE_AUTO 0
+#define MLA_TV_Q8_MERGE_NO_TMEM 1
+#define MLA_TV_Q8_MERGE_ALONE 2
+int mla_tree_verify_q8_debug_merge(const void* q, const void* kv_cache, const float* scales,
+                                   const int32_t* kv_indices, const int32_t* kv_indptr,
+                                   const int64_t* out_cache_loc, const uint8_t* custom_mask,
+                                   const int64_t* mask_indptr, const int64_t* qo_indptr,
+                                   float sm_scale, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t bs, int32_t max_q_per_req,
+                                   int32_t num_heads, int64_t num_slots, int64_t total_q,
+                                   int64_t num_kv_indices, int64_t mask_len, int64_t scale_block,
+                                   int32_t merge_mode, int64_t help_limit_ns, cudaStream_t stream);
+
+/*
  * mla_kv_gather_q8 — mla_tree_verify_kv_gather() for an e4m3 cache with a scale for every
  * row (scale_block = 1): for every index entry i in [kv_indptr[0], kv_indptr[bs]), with
  * j = i - kv_indptr[0],

@@ -7,7 +7,8 @@ The computation runs in ``libmla_tree_verify.so`` (CUDA kernels behind the C ABI
 from .binding import (APPEND_BAD_POS, APPEND_BAD_SCALE, APPEND_BAD_SLOT,  # noqa: F401
                       APPEND_BAD_VALUE, APPEND_PAD_SLOT, DEV_BAD_SCALE, KV_TYPE_BF16,
                       KV_TYPE_E4M3, kv_append, kv_gather_q8, mla_tree_verify_q8,
-                      mla_tree_verify_q8_debug_ex, workspace_bytes_q8)
+                      mla_tree_verify_q8_debug_ex, mla_tree_verify_q8_debug_merge,
+                      Q8_MERGE_ALONE, Q8_MERGE_AUTO, Q8_MERGE_NO_TMEM, workspace_bytes_q8)
 from .binding import (CONV1D_BAD_ACCEPT, CONV1D_BAD_SLOT, CONV1D_DTYPE_BF16,  # noqa: F401
                       CONV1D_DTYPE_F32, CONV1D_PAD_SLOT,
                       DEV_BAD_INDPTR, DEV_BAD_MASK, DEV_BAD_SLOT, DEV_TIMEOUT,

@@ -78,6 +78,8 @@ def load(path: str | None = None):
     lib.mla_tree_verify_q8_debug_ex.argtypes = (lib.mla_tree_verify_q8.argtypes[:-1]
                                                 + [ctypes.POINTER(DebugOpts), vp])
     lib.mla_tree_verify_q8_debug_ex.restype = ctypes.c_int
+    lib.mla_tree_verify_q8_debug_merge.argtypes = lib.mla_tree_verify_q8.argtypes[:-1] + [i32, i64, vp]
+    lib.mla_tree_verify_q8_debug_merge.restype = ctypes.c_int
     lib.mla_kv_gather_q8.argtypes = [vp, vp, i64, vp, i64, vp, i32, vp, vp, i64, i32, vp, vp, vp]
     lib.mla_kv_gather_q8.restype = ctypes.c_int
     lib.mla_kv_append.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, i32, vp, i64, i32, i64,
@@ -214,14 +216,16 @@ def plan_header(workspace) -> dict:
     """The work plan's header as the planner wrote it into ``workspace`` (synchronises):
     total units, units per lane group (capacity), largest tile count, lanes and groups,
     and how many split query tokens (column groups) were merged from TMEM and how many
-    from the workspace."""
+    from the workspace; of the 8-bit kernel also the CTAs that merged as helpers (helps) and
+    the helpers that gave up waiting (helps_left)."""
     import numpy as np
-    h = workspace[:56].cpu().numpy()
+    h = workspace[:64].cpu().numpy()
     i32, i64 = h.view(np.int32), h.view(np.int64)
     return {"error_flags": int(i32[0]), "grid": int(i32[1]), "total_units": int(i64[1]),
             "capacity": int(i64[2]), "max_tiles": int(i64[3]), "tile": int(i32[8]),
             "bs": int(i32[9]), "lanes": int(i32[10]), "groups": int(i32[11]),
-            "merges_tmem": int(i32[12]), "merges_ws": int(i32[13])}
+            "merges_tmem": int(i32[12]), "merges_ws": int(i32[13]),
+            "helps": int(i32[14]), "helps_left": int(i32[15])}
 
 
 def mla_tree_verify_profiled(q, kv_cache, kv_indices, kv_indptr, out_cache_loc, custom_mask,
@@ -391,6 +395,23 @@ def mla_tree_verify_q8_debug_ex(q, kv_cache, scales, kv_indices, kv_indptr, out_
                       scale_block)
     opts = DebugOpts(None, None, int(wait_limit_ns), MERGE_AUTO, int(lanes))
     _on_device(dev, stream, load().mla_tree_verify_q8_debug_ex, (*a, ctypes.byref(opts)))
+
+
+Q8_MERGE_AUTO = 0
+Q8_MERGE_NO_TMEM = 1
+Q8_MERGE_ALONE = 2
+
+
+def mla_tree_verify_q8_debug_merge(q, kv_cache, scales, kv_indices, kv_indptr, out_cache_loc,
+                                   custom_mask, mask_indptr, qo_indptr, sm_scale, out, lse, workspace,
+                                   max_q_per_req, scale_block=1, merge_mode=Q8_MERGE_AUTO,
+                                   help_limit_ns=0, stream=None):
+    """As mla_tree_verify_q8 with a choice of who merges a token's pieces (Q8_MERGE_*) and a limit
+    for the wait of helping CTAs (0: the library's 40 us)."""
+    dev, a = _q8_args(q, kv_cache, scales, kv_indices, kv_indptr, out_cache_loc, custom_mask,
+                      mask_indptr, qo_indptr, sm_scale, out, lse, workspace, max_q_per_req,
+                      scale_block)
+    _on_device(dev, stream, load().mla_tree_verify_q8_debug_merge, (*a, int(merge_mode), int(help_limit_ns)))
 
 
 def kv_append(latent, k_pe, positions, cos_sin, slots, kv_cache, status, scales=None,

@@ -84,8 +84,10 @@ struct RunOpts {
   bool q8 = false;             // kv_cache is e4m3 with these scales
   const float* scales = nullptr;
   int64_t scale_block = 1;
+  uint64_t help_ns = 0;        // 0: kDefaultHelpNs
 };
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
+constexpr uint64_t kDefaultHelpNs = 40000ull;
 
 // CTAs per lane group: the largest power of two up to kMaxLanes that divides the grid and
 // does not exceed a request's column groups (so that a full job can exist).
@@ -181,6 +183,7 @@ int run(const void* q, const void* kv_cache, const int32_t* kv_indices, const in
   p.merge_mode = opt.merge_mode;
   // (the 8-bit kernel counts two clocks a nanosecond, in 64 bits)
   p.wait_ns = opt.wait_ns ? std::min<uint64_t>(opt.wait_ns, UINT64_MAX / 4) : kDefaultWaitNs;
+  p.help_ns = opt.help_ns ? opt.help_ns : kDefaultHelpNs;
   p.num_slots = num_slots;
   p.total_q = total_q;
   p.num_kv_indices = num_kv_indices;
@@ -392,6 +395,29 @@ int mla_tree_verify_q8_debug_ex(const void* q, const void* kv_cache, const float
   opt.scale_block = scale_block;
   opt.wait_ns = opts->wait_limit_ns;
   opt.lanes = opts->lanes;
+  return run(q, kv_cache, kv_indices, kv_indptr, out_cache_loc, custom_mask, mask_indptr,
+             qo_indptr, sm_scale, out, lse, workspace, workspace_bytes, bs, max_q_per_req,
+             num_heads, num_slots, total_q, num_kv_indices, mask_len, opt, stream);
+}
+
+int mla_tree_verify_q8_debug_merge(const void* q, const void* kv_cache, const float* scales,
+                                   const int32_t* kv_indices, const int32_t* kv_indptr,
+                                   const int64_t* out_cache_loc, const uint8_t* custom_mask,
+                                   const int64_t* mask_indptr, const int64_t* qo_indptr,
+                                   float sm_scale, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t bs, int32_t max_q_per_req,
+                                   int32_t num_heads, int64_t num_slots, int64_t total_q,
+                                   int64_t num_kv_indices, int64_t mask_len, int64_t scale_block,
+                                   int32_t merge_mode, int64_t help_limit_ns, cudaStream_t stream) {
+  if (merge_mode < MLA_TV_Q8_MERGE_AUTO || merge_mode > MLA_TV_Q8_MERGE_ALONE || help_limit_ns < 0 ||
+      help_limit_ns > 1000000000)
+    return MLA_TV_ERR_SHAPE;
+  RunOpts opt;
+  opt.q8 = true;
+  opt.scales = scales;
+  opt.scale_block = scale_block;
+  opt.merge_mode = merge_mode;
+  opt.help_ns = (uint64_t)help_limit_ns;
   return run(q, kv_cache, kv_indices, kv_indptr, out_cache_loc, custom_mask, mask_indptr,
              qo_indptr, sm_scale, out, lse, workspace, workspace_bytes, bs, max_q_per_req,
              num_heads, num_slots, total_q, num_kv_indices, mask_len, opt, stream);

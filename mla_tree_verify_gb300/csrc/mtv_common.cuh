@@ -79,7 +79,9 @@ struct WsHeader {
   int32_t groups;        // lane groups: grid / lanes
   uint32_t merges_tmem;  // split tokens merged from TMEM by the CTA of their last piece
   uint32_t merges_ws;    // split tokens merged from the workspace after the last ticket
-  int64_t reserved[9];
+  uint32_t helps;        // 8-bit kernel: CTAs that merged as helpers
+  uint32_t helps_left;   // and helpers that gave up waiting
+  int64_t reserved[8];
 };
 static_assert(sizeof(WsHeader) == 128, "header size");
 
@@ -119,6 +121,8 @@ struct Problem {
   int32_t seg_cost;     // empty units of a job (kSegCost, kSegCostQ8)
   int32_t lanes;        // CTAs per lane group, chosen by the host (the planner records it)
   int32_t merge_mode;   // 0: as timing allows; 1: never from TMEM; 2: from TMEM when it can
+                        // (8-bit kernel: 2: never from TMEM and without helpers)
+  uint64_t help_ns;     // 8-bit kernel: how long a helper waits for the other pieces
   uint64_t wait_ns;     // limit of every bounded wait in the split kernel
   // optional index dump (null unless the debug entry point is used)
   int64_t* dump_slots;  // [sum_b L_b]

@@ -73,6 +73,8 @@ __device__ __forceinline__ void plan_body(const Problem& p, int32_t grid, int32_
     p.hdr->error_flags = 0u;
     p.hdr->merges_tmem = 0u;
     p.hdr->merges_ws = 0u;
+    p.hdr->helps = 0u;
+    p.hdr->helps_left = 0u;
     s_nbad = 0;
   }
   // One request per thread: its six indptr entries are loaded once (one round of

@@ -421,12 +421,11 @@ __device__ __forceinline__ void split_weights(__half2 y, uint32_t dither, uint32
 // - a CTA without takes its ticket as a helper (kHelper in the group's counter), waits for the
 //   other pieces and takes slices until none is left; the CTA of the last piece leaves the merge
 //   to helpers where there are any, and takes the slices itself where there are none.
-// A helper gives up after kHelpNs, in one atomic step with looking whether the group is done,
+// A helper gives up after p.help_ns (40 us), in one atomic step with looking whether the group is done,
 // so that a merge is never left to no one.  (The CTAs of a call need not all be on the GPU at
 // once, beside another kernel's; the limit is then what waiting costs.)  A column's bits do not
 // depend on who merges it.
 constexpr int kHelper = 1 << 16;           // tok_done: finished pieces below, helpers above
-constexpr uint64_t kHelpNs = 40000;
 // From this many pieces on, CTAs without work help.  A merge of two from TMEM takes 6 us, and a
 // helper would have to write its piece first (two: the same times, bs 32 with 8 heads 1% less);
 // three or four alone took 15-19 us after the last piece (three against five: 64 decoding
@@ -554,13 +553,16 @@ __device__ __forceinline__ void merge_slices(const Problem& p, unsigned char* sm
 }
 
 // One thread of a helper: whether it is to merge.
-__device__ __forceinline__ bool help_merge(int* counter, int nseg, volatile int* abort) {
+__device__ __forceinline__ bool help_merge(const Problem& p, int* counter, int nseg, volatile int* abort) {
   const uint64_t t0 = ptx::globaltimer();
   while ((ptx::ld_acquire_gpu(counter) & (kHelper - 1)) < nseg) {
-    if (*abort || ptx::globaltimer() - t0 > kHelpNs)
+    if (*abort || ptx::globaltimer() - t0 >= p.help_ns) {
+      atomicAdd(&p.hdr->helps_left, 1u);
       return (atomicSub(counter, kHelper) & (kHelper - 1)) == nseg;
+    }
     __nanosleep(100);
   }
+  atomicAdd(&p.hdr->helps, 1u);
   return true;
 }
 
@@ -849,9 +851,11 @@ __device__ void softmax_role(const Problem& p, unsigned char* sm, Bars* bars, vo
       }
     }
     const int64_t tok = s.r - q_first;
-    const bool busy = wk.u < wk.u_end || nseg < kHelpPieces;   // no helper: more segments to do
+    // no helper: more segments to do
+    const bool busy = wk.u < wk.u_end || nseg < kHelpPieces || p.merge_mode == 2;
     if (threadIdx.x == kFirstSoftmaxThread)
-      *ticket_s = nseg > 1 && nseg <= kMergeGroup && ptx::ld_acquire_gpu(p.tok_done + tok) == nseg - 1;
+      *ticket_s = nseg > 1 && nseg <= kMergeGroup && p.merge_mode == 0 &&
+                  ptx::ld_acquire_gpu(p.tok_done + tok) == nseg - 1;
     ptx::bar_sync(kSoftmaxBar, kSoftmaxThreads);
     if (*ticket_s) {   // every other piece is done, none of them by a helper
       float* wb = (float*)(sm + kWOff);
@@ -896,7 +900,7 @@ __device__ void softmax_role(const Problem& p, unsigned char* sm, Bars* bars, vo
         const int old = atomicAdd(counter, busy ? 1 : kHelper + 1);
         const bool last = (old & (kHelper - 1)) == nseg - 1;
         if (last) atomicAdd(&p.hdr->merges_ws, 1u);
-        *ticket_s = busy ? last && old < kHelper : last || help_merge(counter, (int)nseg, abort);
+        *ticket_s = busy ? last && old < kHelper : last || help_merge(p, counter, (int)nseg, abort);
       }
       ptx::bar_sync(kSoftmaxBar, kSoftmaxThreads);
       const bool merge = *ticket_s;
