@@ -37,10 +37,6 @@ __device__ __forceinline__ uint32_t unpack2(uint32_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
   return r;
 }
-__device__ __forceinline__ float2 unpack2f(uint32_t c) {
-  const uint32_t h = unpack2(c);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 
 }  // namespace q8
 }  // namespace mtv
