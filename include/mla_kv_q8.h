@@ -69,7 +69,7 @@ extern "C" {
  *                that attention that sees it gives NaN; with given scales the values that are
  *                NaN or infinite become NaN codes; a bf16 row is written as it is);
  *                _BAD_SCALE: a given scale is NaN or
- *                outside [2^-40, 2^40] (the token is skipped)
+ *                outside [2^-40, 2^40] (the token is skipped like padding)
  *
  * Returns MLA_TV_OK (n = 0 enqueues nothing), or before enqueuing anything MLA_TV_ERR_NULL /
  * _SHAPE (n < 0, num_slots outside [1, INT32_MAX], max_pos < 1, an unknown cache_type, a

@@ -188,7 +188,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int64_t i, int6
 // 53); halves: four lanes a head, 16 bytes of each half (with a shuffle between eight lanes,
 // 32768 tokens of 8 heads took 32 us against 29).  Slot j of the sixteen is head h0 + j of token
 // i, or with kMany (heads <= 8) head j % heads of token i + j / heads.
-template <bool kInter, bool kMany>
+template <bool kGiven, bool kInter, bool kMany>
 __device__ __forceinline__ void rotate_heads(const AppendArgs& a, int64_t i, int h0) {
   constexpr int kLanes = kInter ? 8 : 4, kParts = kInter ? 1 : 2;   // lanes a head, loads a lane
   constexpr int kHeads = 32 / kLanes, kRounds = kHeadsPerItem / kHeads, kPairs = 4 * kParts;
@@ -214,7 +214,8 @@ __device__ __forceinline__ void rotate_heads(const AppendArgs& a, int64_t i, int
   int64_t slot[kTables], pos[kTables];
 #pragma unroll
   for (int k = 0; k < kTables; ++k)
-    live[k] = (!kMany || on[k]) && token(a, tok[k], false, slot[k], pos[k]);
+    live[k] = (!kMany || on[k]) && token(a, tok[k], false, slot[k], pos[k]) &&
+              (!kGiven || q8::scale_ok(a.scales[slot[k] >> a.scale_shift]));
 #pragma unroll
   for (int k = 0; k < kTables; ++k) {
     if (!live[k]) continue;
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kAppendThreads, kMany ? 4 : kInter ? 6 : 5)
   if (part < row_items) {
     append_rows<kType, kGiven, kInter, kRows>(a, i + part * kRows, min((int64_t)a.n, i + a.bundle));
   } else {
-    rotate_heads<kInter, kMany>(a, i, (part - row_items) * kHeadsPerItem);
+    rotate_heads<kGiven, kInter, kMany>(a, i, (part - row_items) * kHeadsPerItem);
   }
 }
 

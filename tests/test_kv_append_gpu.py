@@ -178,6 +178,17 @@ def test_bad_given_scales_are_skipped():
     assert int(c.status) == mtv.APPEND_BAD_SCALE
 
 
+@pytest.mark.parametrize("heads", [1, 8, 64])
+@pytest.mark.parametrize("inter", [True, False])
+def test_queries_of_tokens_with_bad_given_scales_are_left_alone(heads, inter):
+    c = Case(100, heads, block=16, inter=inter, seed=15)
+    bad = (c.slots[3] // 16).item()
+    c.scales[bad] = 2.0 ** 41
+    c.run()
+    c.check(True, skip=(c.slots // 16 == bad).nonzero()[:, 0].tolist())
+    assert int(c.status) == mtv.APPEND_BAD_SCALE
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("dim", [0, 511, 520])
 def test_nonfinite_rows(value, dim):
