@@ -134,3 +134,44 @@ def test_a_row_without_values_that_outweighs_the_others(first):
     only.kv[at] = 0
     out, lse = only.run()
     assert not out.any() and float((lse - math.log(201)).abs().max()) < 1e-5
+
+
+@pytest.mark.parametrize("heads", [64, 8])
+@pytest.mark.parametrize("order", [6, 9, 12, 15])
+def test_queries_with_one_large_value(order, heads):
+    """A query value 2^order times the row's others, in a dim that no key uses: the others are exact
+    down to 2^-9 of it, and within 2^-17 of it below."""
+    b = Batch([500, 130], [2, 1], heads, seed=37)
+    b.q[..., 5] = 2.0 ** order
+    b.kv[torch.cat([b.kv_indices.long(), b.out_cache_loc]), 5] = 0
+    out, lse = b.run()
+    q8_tight.check(b, out, lse)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches_of_every_kind_within_tight_tolerances(seed):
+    """Steep and flat softmaxes, a first key that outweighs the rest (0 to 24 binary orders), scales over 12
+    binary orders, rows without values, masks that are no trees."""
+    g = torch.Generator().manual_seed(2000 + seed)
+    ri = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    top = [60, 700, 6000, 25000][seed % 4]
+    n = ri(1, 5)
+    P, T = [ri(1, top) for _ in range(n)], [ri(1, [3, 12][seed % 2]) for _ in range(n)]
+    b = Batch(P, T, 64 if seed % 3 else 8, [1, 1, 64][ri(0, 2)], seed=60 + seed)
+    b.mask &= (torch.rand(b.mask.shape, generator=g).cuda() < [1.1, 0.5][ri(0, 1)]).to(torch.uint8)
+    b.scales *= torch.exp2(torch.randint(-6, 7, b.scales.shape, generator=g).float()).cuda()
+    at = b.kv_indices.long()
+    b.kv[at[torch.rand(at.shape, generator=g).cuda() < 0.05], :LATENT] = 0
+    q_small = 2.0 ** -ri(0, 6)
+    b.q *= q_small
+    if ri(0, 2):
+        first = b.kv_indptr[:-1].long()
+        b.kv[at[first]] = 0
+        b.kv[at[first], :LATENT] = torch.randint(0x30, 0x38, (n, LATENT), generator=g, dtype=torch.uint8).cuda()
+        b.kv[at, 3] = 0
+        b.kv[at[first], 3] = 0x70                       # 128
+        b.scales[at[first] // b.block] = 0.01
+        b.q[..., 3] = ri(0, 24) * math.log(2.0) / (1.28 / math.sqrt(192.0))
+    out, lse = b.run()
+    q8_tight.check(b, out, lse)
+    assert b.flags() == 0
