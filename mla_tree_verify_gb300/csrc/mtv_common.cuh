@@ -25,9 +25,9 @@ constexpr int kNsplit = 64;    // at most this many partials per query token
 constexpr int kSegCost = 1;    // of the 16-bit kernel (the 8-bit one's: kSegCostQ8)
 constexpr int kRowBytes = kDqk * 2;
 // With tiles at 2.3 us and a segment's start and end at about 9, four of them: 64 decoding
-// requests 100.3 us a call against 101.0 with three and 104.2 with two, bs 32 with 8 heads 88.6
-// against 89.7 and 91.9, bs 64, 8k-64k 2515 against 2515 and 2536, bs 8, 1k-4k 80.3 against 80.2 and
-// 79.9; with five 102.2, 88.6, 2519 and 80.7.
+// requests 95.3 us a call against 97.1 with three and 99.8 with two, bs 32 with 8 heads 86.3
+// against 86.6 and 88.7, bs 64, 8k-64k 2520 against 2519 and 2546, bs 8, 1k-4k 76.0 against 75.3 and
+// 75.5; with five 97.8, 86.5, 2530 and 76.4.
 constexpr int kSegCostQ8 = 4;
 // Lanes: split CTAs that walk one unit range together, each on a different column group
 // (or a different part of one column group's key tiles) of the same request, so that a

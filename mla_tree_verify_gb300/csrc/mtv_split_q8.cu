@@ -50,10 +50,10 @@
 // of warp 12 issues the scores and one of warp 13 the values, so that neither waits for the
 // other's turn; warps 4-11 run the softmax, the rescale and the epilogue.
 //
-// Measured.  64 requests of 8k-64k keys, trees of 1 to 16 drafts: 2.53 ms, 1.00 PFLOP/s of
+// Measured.  64 requests of 8k-64k keys, trees of 1 to 16 drafts: 2.52 ms, 1.01 PFLOP/s of
 // attention arithmetic, 53% of the measured bf16 matrix peak; one request of 185k keys with 16
-// drafts: 374 us, 58%.  A tile takes about 2.2 us (4300 clocks at 64 heads): its 50 MMAs 2750
-// clocks when nothing is waited for, the softmax 1700.  What bounds it is the cycle of one tile
+// drafts: 373 us, 58%.  A tile takes about 2.3 us (4400 clocks at 64 heads): its 50 MMAs 2750
+// clocks when nothing is waited for, the softmax 1650-1850.  What bounds it is the cycle of one tile
 // buffer, two tiles long: values 3000 clocks (the scores of the next tile share the tensor
 // cores), the refill of the chunks released last 1800, their scores 600, the softmax, and about
 // 600 of hand-offs.  A third buffer, which would take it off the path, does not fit beside q.
@@ -427,9 +427,10 @@ __device__ __forceinline__ void split_weights(__half2 y, uint32_t dither, uint32
 // depend on who merges it.
 constexpr int kHelper = 1 << 16;           // tok_done: finished pieces below, helpers above
 // From this many pieces on, CTAs without work help.  A merge of two from TMEM takes 6 us, and a
-// helper would have to write its piece first (two: the same times, bs 32 with 8 heads 1% less);
+// helper would have to write its piece first (two: the same times);
 // three or four alone took 15-19 us after the last piece (three against five: 64 decoding
-// requests 101.6 us a call against 109, bs 8, 1k-4k 83.3 against 87.8).
+// requests 95.3 us a call against 100.7, bs 8, 1k-4k 76.0 against 79.4, bs 32 with 8 heads 86.3
+// against 91.5).
 constexpr int kHelpPieces = 3;
 constexpr int kSlices = 8;
 constexpr int kSliceCols = kHeads / kSlices;
